@@ -127,7 +127,7 @@ __global__ __launch_bounds__(256) void mm_general_kernel(MmArgs g) {
             const int n = min(n0 + wn * 32 + 8 * (i >> 2) + 4 * half + (i & 3), g.N - 1);
             const float sb =
                 scale_factor<ST>(load_scale<ST>(g.bs, (int64_t)(n >> g.b_shift) * g.bs_row + kb * g.bs_blk));
-            acc[i] = __builtin_fmaf(p[i] * sa, sb, acc[i]);
+            acc[i] += scaled(p[i], sa, sb);
         }
         __syncthreads();
     }
@@ -190,6 +190,7 @@ __global__ __launch_bounds__(1024) void mm_skinny_kernel(MmArgs g) {
     const int64_t as_row = (int64_t)(m >> g.a_shift) * g.as_row;
     v4f acc{0, 0, 0, 0};
 
+    constexpr bool HWS = ST == RNS_T_E8M0 && !WIDE;          // the instruction applies the scales: those of its lane's rows
     struct Batch {
         Frag b[U], a[U];
         uint32_t sa[U], sb[U][4];
@@ -207,7 +208,9 @@ __global__ __launch_bounds__(1024) void mm_skinny_kernel(MmArgs g) {
         for (int u = 0; u < U; u++) {
             const int kb = min(kb0 + u, kb_all - 1);
             x.sa[u] = load_scale<ST>(g.as, as_row + kb * g.as_blk);
-            if (g.b_shift) {
+            if (HWS) {
+                x.sb[u][0] = load_scale<ST>(g.bs, (min(n0 + l16, g.N - 1) >> g.b_shift) * g.bs_row + kb * g.bs_blk);
+            } else if (g.b_shift) {
                 // 16 rows that start at a multiple of 16 share a block
                 x.sb[u][0] = load_scale<ST>(g.bs, (n0 >> 7) * g.bs_row + kb * g.bs_blk);
             } else {
@@ -230,6 +233,11 @@ __global__ __launch_bounds__(1024) void mm_skinny_kernel(MmArgs g) {
         for (int u = 0; u < U; u++) {
             if (kb0 + u >= kb_all) break;                    // a block past the end adds nothing, whatever its scale
             const v8i wb = frag_words(x.b[u]), wa = frag_words(x.a[u]);
+            if constexpr (HWS) {
+                acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wb, wa, acc, 0, AT == RNS_T_E5M2, 0, (int)x.sb[u][0], 0,
+                                                                       (int)x.sa[u]);
+                continue;
+            }
             v4f p{0, 0, 0, 0};
             if constexpr (WIDE) {
 #pragma unroll
@@ -239,10 +247,10 @@ __global__ __launch_bounds__(1024) void mm_skinny_kernel(MmArgs g) {
             } else {
                 p = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wb, wa, p, 0, AT == RNS_T_E5M2, 0, 0, 0, 0);
             }
+            const float sa = scale_factor<ST>(x.sa[u]);
 #pragma unroll
             for (int e = 0; e < 4; e++)
-                acc[e] = __builtin_fmaf(p[e] * scale_factor<ST>(x.sa[u]), scale_factor<ST>(x.sb[u][g.b_shift ? 0 : e]),
-                                        acc[e]);
+                acc[e] += scaled(p[e], sa, scale_factor<ST>(x.sb[u][g.b_shift ? 0 : e]));
         }
     };
     // While there are as many batches again, no load stands behind a branch: one that may not have been issued would
@@ -300,7 +308,8 @@ __global__ __launch_bounds__(1024) void mm_skinny_kernel(MmArgs g) {
 //
 // HWS: both scale arrays are powers of two, which v_mfma_scale applies to the
 // operands itself.  Otherwise a block's product starts from zero and is scaled
-// into the sum by fused multiply-adds (BROW: b's scales differ by row).
+// into the sum by fused multiply-adds (BROW: b's scales differ by row); a block
+// with scales far from one first, by significands and exponents.
 //
 // A block's fragments cost more to read from LDS (T = 128: 96 KiB at 128 bytes
 // a clock, 0.32 us) than to multiply (0.21 us at the instructions' rate);
@@ -386,7 +395,7 @@ __global__ __launch_bounds__(T * 4 * KG) void mm_tile_kernel(MmArgs g) {
     }
     // scales: the waves in turn fetch 64 rows of a, then of b, each; the second half of the waves the same once more
     // (every wave has as many loads)
-    const bool of_a = (wave & (T / 64)) == 0, e8m0 = HWS || g.e8m0;
+    const bool of_a = (wave & (T / 64)) == 0, e8m0 = HWS || (WIDE && g.e8m0);   // (8-bit instructions: HWS)
     const int srow = (T == 128 ? (wave & 1) * 64 : 0) + lane, es = e8m0 ? 1 : 4;
     const uint8_t *sbase = (const uint8_t *)(of_a ? g.as : g.bs);
     const int64_t sblk = (of_a ? g.as_blk : g.bs_blk) * es;
@@ -501,6 +510,18 @@ __global__ __launch_bounds__(T * 4 * KG) void mm_tile_kernel(MmArgs g) {
             }
         } else {
             v4f p[FI][2];
+            float s[FI], fb[2][4];                           // BROW: a's scales and b's; otherwise the products of both
+            Extent x;
+            auto look = [&](int i) {
+                s[i] = BROW ? factor(r.sa[i]) : factor(r.sa[i]) * factor(r.sb[0]);
+                x.add(s[i]);
+                if constexpr (BROW)
+#pragma unroll
+                    for (int k = i * 8 / FI; k < (i + 1) * 8 / FI; k++) {
+                        fb[k >> 2][k & 3] = factor(sb[k >> 2][k & 3]);
+                        x.add(fb[k >> 2][k & 3]);
+                    }
+            };
             if constexpr (WIDE) {
 #pragma unroll
                 for (int q = 0; q < 4; q++) {
@@ -515,7 +536,10 @@ __global__ __launch_bounds__(T * 4 * KG) void mm_tile_kernel(MmArgs g) {
                         for (int j = 0; j < 2; j++)
                             p[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
                                 wb[j], wa[i], q == 0 ? v4f{0, 0, 0, 0} : p[i][j], 0, 0, 0);
-                    if (q < FI) requests(q);
+                    if (q < FI) {
+                        look(q);
+                        requests(q);
+                    }
                 }
             } else {
 #pragma unroll
@@ -524,19 +548,32 @@ __global__ __launch_bounds__(T * 4 * KG) void mm_tile_kernel(MmArgs g) {
                     for (int j = 0; j < 2; j++)
                         p[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
                             r.fb[j], r.fa[i], v4f{0, 0, 0, 0}, 0, AT == RNS_T_E5M2, 0, 0, 0, 0);
+                    look(i);                                 // while the matrix cores are at work
                     requests(i);
                 }
             }
+            if (__any(BROW ? x.beyond(kScaleLow, kScaleHigh) : x.beyond(kSmallestNormal, kLargestFinite))) {
+                // the products scaled, and factors of one
 #pragma unroll
-            for (int i = 0; i < FI; i++) {
-                const float sa = factor(r.sa[i]), s = BROW ? sa : sa * factor(r.sb[0]);
+                for (int i = 0; i < FI; i++)
+#pragma unroll
+                    for (int j = 0; j < 2; j++)
+#pragma unroll
+                        for (int e = 0; e < 4; e++)
+                            p[i][j][e] = scaled(p[i][j][e], factor(r.sa[i]), BROW ? fb[j][e] : factor(r.sb[0]));
+#pragma unroll
+                for (int i = 0; i < FI; i++) s[i] = 1.f;
+#pragma unroll
+                for (int k = 0; k < 8; k++) fb[k >> 2][k & 3] = 1.f;
+            }
+#pragma unroll
+            for (int i = 0; i < FI; i++)
 #pragma unroll
                 for (int j = 0; j < 2; j++)
 #pragma unroll
                     for (int e = 0; e < 4; e++)
-                        acc[i][j][e] = BROW ? __builtin_fmaf(p[i][j][e] * s, factor(sb[j][e]), acc[i][j][e])
-                                            : __builtin_fmaf(p[i][j][e], s, acc[i][j][e]);
-            }
+                        acc[i][j][e] = BROW ? __builtin_fmaf(p[i][j][e] * s[i], fb[j][e], acc[i][j][e])
+                                            : __builtin_fmaf(p[i][j][e], s[i], acc[i][j][e]);
         }
     };
 
@@ -657,6 +694,27 @@ __global__ __launch_bounds__(T * 4 * KG) void mm_tile_kernel(MmArgs g) {
 // powers of two, 2.2 to 2.4 PFLOP/s), 520 with binary32 scales, whose vector
 // instructions share the issue slots; the library's product with one scale for
 // each whole operand takes 390 to 430.  4096 x 4096 x 4096: 61 us, 51 there.
+// A scale as a power of two 2^(e - 127) that the instruction can apply, times
+// the rest, which is below 4 and at least 1 where the scale is normal.
+struct Split {
+    uint32_t e;
+    float r;
+};
+__device__ __forceinline__ Split split_scale(float s) {
+    const uint32_t e = min(max((__float_as_uint(s) >> 23) & 0xff, 1u), 253u);     // so that the inverse is normal too
+    return Split{e, s * __uint_as_float((254 - e) << 23)};
+}
+// b times a, times 2^(eb - 127) and 2^(byte i of ea - 127).
+template <int AT>
+__device__ __forceinline__ v4f scaled_product(const v8i &b, const v8i &a, int i, uint32_t eb, uint32_t ea) {
+    constexpr v4f zero{0, 0, 0, 0};
+    constexpr int type = AT == RNS_T_E5M2;
+    if (i == 0) return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b, a, zero, 0, type, 0, (int)eb, 0, (int)ea);
+    if (i == 1) return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b, a, zero, 0, type, 0, (int)eb, 1, (int)ea);
+    if (i == 2) return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b, a, zero, 0, type, 0, (int)eb, 2, (int)ea);
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b, a, zero, 0, type, 0, (int)eb, 3, (int)ea);
+}
+
 template <int AT, bool HWS>
 __global__ __launch_bounds__(512) void mm_big_kernel(MmArgs g) {
     // 256 rows of a, 256 rows of b, 8 chunks each, twice; then four places for scales.  One array: beside a second
@@ -751,23 +809,40 @@ __global__ __launch_bounds__(512) void mm_big_kernel(MmArgs g) {
         const uint32_t a = (at0 ^ (32 * (f & 3))) + region + f * 2048;
         return frag_words(Frag{*(lds_chunk)(lds0 + a), *(lds_chunk)(lds0 + (a ^ 16))});
     };
-    uint32_t sa[4], sb[4];
-    float s[4] = {0, 0, 0, 0};                               // a's scales times b's
+    // Binary32 scales: the instruction takes their powers of two (a's four in the bytes of ea, b's in eb), which it applies
+    // before anything is rounded, so that nothing leaves binary32's range before the result does; what is left of b's
+    // scale is rb, and of both s.
+    uint32_t sa[4], sb[4], ea = 0x7f7f7f7f, eb = 127;
+    float s[4] = {0, 0, 0, 0}, rb = 1;
     auto scale_in = [&](v4f &to, const v4f &from, float f) {
 #pragma unroll
         for (int e = 0; e < 4; e++) to[e] = __builtin_fmaf(from[e], f, to[e]);
     };
-    // the scales of block kb for rows 64 h .. of this wave
-    auto take_scales = [&](int kb, int h) {
+    // the scales of block kb for rows 64 h .. of this wave, as they are; asked for before the fragments, they are worked on
+    // while those are on their way
+    auto read_scales = [&](int kb, int h) {
         const uint32_t *sc = scales[kb & 3];
+#pragma unroll
+        for (int i = 0; i < 4; i++) sa[i] = sc[wm * 128 + h * 64 + i * 16 + l16];
         if (HWS && h == 0)
 #pragma unroll
             for (int j = 0; j < 4; j++) sb[j] = sc[256 + wn * 64 + 16 * j + l16];
         if (!HWS && h == 0) sb[0] = sc[256 + wn * 64];
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    auto split_scales = [&](int h) {
+        if constexpr (!HWS) {
+            if (h == 0) {
+                const Split b = split_scale(__uint_as_float(sb[0]));
+                eb = b.e;
+                rb = b.r;
+            }
 #pragma unroll
-        for (int i = 0; i < 4; i++) {
-            sa[i] = sc[wm * 128 + h * 64 + i * 16 + l16];
-            if (!HWS) s[i] = __uint_as_float(sa[i]) * __uint_as_float(sb[0]);
+            for (int i = 0; i < 4; i++) {
+                const Split a = split_scale(__uint_as_float(sa[i]));
+                ea = i == 0 ? a.e : ea | a.e << 8 * i;
+                s[i] = a.r * rb;
+            }
         }
     };
     // the products that a compute phase left unscaled: the last ones of row fragment 3
@@ -791,8 +866,7 @@ __global__ __launch_bounds__(512) void mm_big_kernel(MmArgs g) {
                 acc[4 * h + i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
                     fb[j], fa[i], acc[4 * h + i][j], 0, AT == RNS_T_E5M2, 0, (int)sb[j], 0, (int)sa[i]);
             } else {
-                p[t & LAG] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fb[j], fa[i], v4f{0, 0, 0, 0}, 0,
-                                                                              AT == RNS_T_E5M2, 0, 0, 0, 0);
+                p[t & LAG] = scaled_product<AT>(fb[j], fa[i], i, eb, ea);
                 if (t >= LAG) {
                     const int u = t - LAG;
                     scale_in(acc[4 * h + (u >> 2)][u & 3], p[u & LAG], s[u >> 2]);
@@ -808,10 +882,11 @@ __global__ __launch_bounds__(512) void mm_big_kernel(MmArgs g) {
         constexpr bool S = decltype(steady)::value;
         const uint32_t A = (j & 1) * 65536 + wm * 16384, B = (j & 1) * 65536 + 32768 + wn * 8192;
         // read 1
+        read_scales(j, 0);
 #pragma unroll
         for (int f = 0; f < 4; f++) fb[f] = fragment(B, f), fa[f] = fragment(A, f);
         finish(1);
-        take_scales(j, 0);
+        split_scales(0);
         if (S || j + 1 < kbs) wait_loads<7>();
         else wait_loads<0>();
         if (!S && straddle && j == kbs - 1) trim(j, false);
@@ -823,10 +898,11 @@ __global__ __launch_bounds__(512) void mm_big_kernel(MmArgs g) {
         });
         fence();
         // read 2
+        read_scales(j, 1);
 #pragma unroll
         for (int f = 0; f < 4; f++) fa[f] = fragment(A, 4 + f);
         finish(0);
-        take_scales(j, 1);
+        split_scales(1);
         if (S || j + 1 < kbs) wait_loads<2>();
         else wait_loads<0>();
         if (!S && straddle && j + 2 == kbs) trim(j + 1, true);

@@ -39,6 +39,28 @@ __device__ __forceinline__ float scale_factor(uint32_t w) {
     else return e8m0_factor(w);
 }
 
+// A block's product p (0 or 2^-25 .. 2^32 in magnitude) times both scales.
+// By two multiplications p sa or sa sb can overflow, or fall below the smallest
+// normal number, where p sa sb does neither; so the significands are
+// multiplied, and the exponents added.
+__device__ __forceinline__ float scaled(float p, float sa, float sb) {
+    const float x = p * __builtin_amdgcn_frexp_mantf(sa) * __builtin_amdgcn_frexp_mantf(sb);
+    return __builtin_amdgcn_ldexpf(x, __builtin_amdgcn_frexp_expf(sa) + __builtin_amdgcn_frexp_expf(sb));
+}
+// Where multiplications have to be few, scales are looked at first: with both
+// within 2^-46 .. 2^46, or their product normal, two multiplications (or the
+// one by the product) stay in range.
+constexpr float kScaleLow = 1.42108547e-14f, kScaleHigh = 7.03687442e13f;         // 2^-46, 2^46
+constexpr float kSmallestNormal = 1.17549435e-38f, kLargestFinite = 3.4028235e38f;
+struct Extent {
+    float low = kScaleHigh, high = kScaleLow;
+    __device__ __forceinline__ void add(float s) {           // a NaN changes nothing, and needs no care
+        low = fminf(low, fabsf(s));
+        high = fmaxf(high, fabsf(s));
+    }
+    __device__ __forceinline__ bool beyond(float l, float h) const { return low < l || high > h; }
+};
+
 __device__ __forceinline__ uint32_t bf16_bits(float f) {
     const __bf16 h = (__bf16)f;                    // nearest, ties to even
     return __builtin_bit_cast(uint16_t, h);

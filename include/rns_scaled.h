@@ -91,7 +91,9 @@ int rns_block_quantize(int64_t R, int64_t C, const void *x, int32_t x_type, int6
  * [N][K], both contracted along their columns, with
  *   Y[m][n] = sum_blocks sa(m, blk) sb(n, blk) sum_{k in blk} va(m, k) vb(n, k),
  * the scaled total in binary32, rounded once to y_type (RNS_T_F32, BF16 or F16;
- * ldy elements between rows).  For y_type RNS_T_F32 the inner sums are binary32
+ * ldy elements between rows).  Scales may be as far from one as they can be
+ * written: nothing overflows before a block's scaled product does, and one below
+ * 2^-120 is kept to 2^-144.  For y_type RNS_T_F32 the inner sums are binary32
  * sums of exact products; for the 16-bit types they are the 8-bit matrix
  * instructions', which keep each product to about 2^-14 of the largest of the
  * 64 or 128 added at a time.  b's values are
