@@ -36,11 +36,17 @@ struct MoeArgs {
 struct WeightFrag {
     v4u lo, hi;             // 32 bytes
 };
-__device__ __forceinline__ void widen(const WeightFrag &w, v8bf (&o)[4]) {
-    o[0] = widen8<RNS_T_E4M3>(w.lo[0], w.lo[1]);
-    o[1] = widen8<RNS_T_E4M3>(w.lo[2], w.lo[3]);
-    o[2] = widen8<RNS_T_E4M3>(w.hi[0], w.hi[1]);
-    o[3] = widen8<RNS_T_E4M3>(w.hi[2], w.hi[3]);
+// The power of two in a block's scale goes into the weights: their products are as large as the results are, however
+// large the tokens' entries.
+__device__ __forceinline__ void widen(const WeightFrag &w, float power, v8bf (&o)[4]) {
+    o[0] = widen8<RNS_T_E4M3>(w.lo[0], w.lo[1], power);
+    o[1] = widen8<RNS_T_E4M3>(w.lo[2], w.lo[3], power);
+    o[2] = widen8<RNS_T_E4M3>(w.hi[0], w.hi[1], power);
+    o[3] = widen8<RNS_T_E4M3>(w.hi[2], w.hi[3], power);
+}
+template <int ST>
+__device__ __forceinline__ Split split_weight(uint32_t s) {
+    return split_scale<127 - 100, 127 + 100>(scale_factor<ST>(s));
 }
 // Bytes `at` .. at + 31 of a row of `len` bytes (a multiple of 16), and entries
 // at .. at + 31 of a bfloat16 row of `len`.  What lies past the row's end is
@@ -360,17 +366,17 @@ __global__ __launch_bounds__(kInThreads) void moe_in_kernel(MoeArgs g) {
                     trim(f.up, at, H);
                     trim(f.col, at, H);
                 }
-                widen(f.gate, w);
+                const Split sg = split_weight<ST>(f.sg), su = split_weight<ST>(f.su);
+                widen(f.gate, sg.power(), w);
 #pragma unroll
                 for (int i = 0; i < 4; i++) pg = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[i], f.col[i], pg, 0, 0, 0);
-                widen(f.up, w);
+                widen(f.up, su.power(), w);
 #pragma unroll
                 for (int i = 0; i < 4; i++) pu = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[i], f.col[i], pu, 0, 0, 0);
-                const float fg = scale_factor<ST>(f.sg), fu = scale_factor<ST>(f.su);
 #pragma unroll
                 for (int i = 0; i < 4; i++) {
-                    ag[i] = __builtin_fmaf(pg[i], fg, ag[i]);
-                    au[i] = __builtin_fmaf(pu[i], fu, au[i]);
+                    ag[i] = __builtin_fmaf(pg[i], sg.r, ag[i]);
+                    au[i] = __builtin_fmaf(pu[i], su.r, au[i]);
                 }
             };
             Fetched f[2];
@@ -481,8 +487,8 @@ __global__ __launch_bounds__(kOutThreads) void moe_out_kernel(MoeArgs g) {
         const bool tail = (p.kb + 1) * 128 > I;
         v8bf w[4];
         if (tail) trim(f.w, at, I);
-        widen(f.w, w);
-        const float factor = scale_factor<ST>(f.s);
+        const Split scale = split_weight<ST>(f.s);
+        widen(f.w, scale.power(), w);
         const int base = __builtin_amdgcn_readlane(of_base, p.slot), end = __builtin_amdgcn_readlane(of_end, p.slot);
         for (int t0 = 0; base + t0 < end; t0 += 16) {        // more than 16 tokens: the others with the weights at hand
             if (t0 > 0) fetch_columns(p, t0, c);
@@ -500,7 +506,7 @@ __global__ __launch_bounds__(kOutThreads) void moe_out_kernel(MoeArgs g) {
                 v4f &to = sum[wave][c.token][quad];
                 v4f s = to;
 #pragma unroll
-                for (int i = 0; i < 4; i++) s[i] = __builtin_fmaf(o[i], factor, s[i]);
+                for (int i = 0; i < 4; i++) s[i] = __builtin_fmaf(o[i], scale.r, s[i]);
                 to = s;
             }
         }

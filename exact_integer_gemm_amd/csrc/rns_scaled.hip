@@ -694,16 +694,6 @@ __global__ __launch_bounds__(T * 4 * KG) void mm_tile_kernel(MmArgs g) {
 // powers of two, 2.2 to 2.4 PFLOP/s), 520 with binary32 scales, whose vector
 // instructions share the issue slots; the library's product with one scale for
 // each whole operand takes 390 to 430.  4096 x 4096 x 4096: 61 us, 51 there.
-// A scale as a power of two 2^(e - 127) that the instruction can apply, times
-// the rest, which is below 4 and at least 1 where the scale is normal.
-struct Split {
-    uint32_t e;
-    float r;
-};
-__device__ __forceinline__ Split split_scale(float s) {
-    const uint32_t e = min(max((__float_as_uint(s) >> 23) & 0xff, 1u), 253u);     // so that the inverse is normal too
-    return Split{e, s * __uint_as_float((254 - e) << 23)};
-}
 // b times a, times 2^(eb - 127) and 2^(byte i of ea - 127).
 template <int AT>
 __device__ __forceinline__ v4f scaled_product(const v8i &b, const v8i &a, int i, uint32_t eb, uint32_t ea) {
@@ -833,13 +823,13 @@ __global__ __launch_bounds__(512) void mm_big_kernel(MmArgs g) {
     auto split_scales = [&](int h) {
         if constexpr (!HWS) {
             if (h == 0) {
-                const Split b = split_scale(__uint_as_float(sb[0]));
+                const Split b = split_scale<1, 253>(__uint_as_float(sb[0]));
                 eb = b.e;
                 rb = b.r;
             }
 #pragma unroll
             for (int i = 0; i < 4; i++) {
-                const Split a = split_scale(__uint_as_float(sa[i]));
+                const Split a = split_scale<1, 253>(__uint_as_float(sa[i]));
                 ea = i == 0 ? a.e : ea | a.e << 8 * i;
                 s[i] = a.r * rb;
             }

@@ -47,6 +47,19 @@ __device__ __forceinline__ float scaled(float p, float sa, float sb) {
     const float x = p * __builtin_amdgcn_frexp_mantf(sa) * __builtin_amdgcn_frexp_mantf(sb);
     return __builtin_amdgcn_ldexpf(x, __builtin_amdgcn_frexp_expf(sa) + __builtin_amdgcn_frexp_expf(sb));
 }
+// A scale as a power of two 2^(e - 127) that an instruction can apply to its
+// operand, times the rest, which is below 2 and at least 1 where the scale's
+// own exponent is one of LO .. HI (1 .. 253, so that the inverse is normal too).
+struct Split {
+    uint32_t e;
+    float r;
+    __device__ __forceinline__ float power() const { return __uint_as_float(e << 23); }
+};
+template <int LO, int HI>
+__device__ __forceinline__ Split split_scale(float s) {
+    const uint32_t e = min(max((__float_as_uint(s) >> 23) & 0xff, (uint32_t)LO), (uint32_t)HI);
+    return Split{e, s * __uint_as_float((254 - e) << 23)};
+}
 // Where multiplications have to be few, scales are looked at first: with both
 // within 2^-46 .. 2^46, or their product normal, two multiplications (or the
 // one by the product) stay in range.
@@ -74,20 +87,20 @@ __device__ __forceinline__ float f16_float(uint32_t b) {
     return (float)__builtin_bit_cast(_Float16, (uint16_t)b);
 }
 
-// Eight 8-bit values (two words) as bfloat16, which holds every one of them.
+// Eight 8-bit values (two words), times a power of two of 2^-100 .. 2^100, as bfloat16, which holds every one of them.
 template <int TYPE>
-__device__ __forceinline__ v8bf widen8(uint32_t w0, uint32_t w1) {
+__device__ __forceinline__ v8bf widen8(uint32_t w0, uint32_t w1, float scale = 1.0f) {
     v2bf a, b, c, d;
     if constexpr (TYPE == RNS_T_E4M3) {
-        a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w0, 1.0f, false);
-        b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w0, 1.0f, true);
-        c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w1, 1.0f, false);
-        d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w1, 1.0f, true);
+        a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w0, scale, false);
+        b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w0, scale, true);
+        c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w1, scale, false);
+        d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w1, scale, true);
     } else {
-        a = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(w0, 1.0f, false);
-        b = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(w0, 1.0f, true);
-        c = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(w1, 1.0f, false);
-        d = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(w1, 1.0f, true);
+        a = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(w0, scale, false);
+        b = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(w0, scale, true);
+        c = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(w1, scale, false);
+        d = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(w1, scale, true);
     }
     return v8bf{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
