@@ -27,6 +27,7 @@ template <bool E5M2>
 struct Format {
     static constexpr float largest = E5M2 ? 57344.f : 448.f;
     static constexpr int top = E5M2 ? 15 : 8;
+    static constexpr float small_scale = E5M2 ? 0x1p-86f : 0x1p-93f;    // see `quotient`
 };
 
 // A block's scale: the binary32 number, or the biased exponent; and what its
@@ -40,14 +41,16 @@ struct Scale {
 // x over s, correctly rounded, without the divider's full sequence: with r =
 // fl(1 / s), one correction by the exact remainder brings x r to within one
 // unit in the last place, and from such a value the next gives the rounded
-// quotient.  The remainders are exact while nothing underflows or overflows
-// (scales of at least 2^-96, finite x).
+// quotient, as long as the remainders are exact: their last bit is that of q
+// times that of s, which has to be 2^-149 or more.  The smallest q whose
+// rounding matters is half the type's smallest step, 2^-10 for E4M3 and 2^-17
+// for E5M2, with last bits 2^-33 and 2^-40; so s has to be at least 2^-93 or
+// 2^-86, whose last bits are 2^-116 and 2^-109.  (Smaller q all become zero.)
 __device__ __forceinline__ float quotient(float x, float s, float r) {
     float q = x * r;
     q = __builtin_fmaf(__builtin_fmaf(-q, s, x), r, q);
     return __builtin_fmaf(__builtin_fmaf(-q, s, x), r, q);
 }
-constexpr float kSmallScale = 1.2621774e-29f;               // 2^-96
 
 // The smallest 2^e with amax <= 1.75 * 2^(top + e): e = exponent(amax) - top,
 // one more where amax's mantissa exceeds 1.75 (then adding 2^21 - 1 to its
@@ -145,7 +148,7 @@ __device__ __forceinline__ float grow(float m, float x) { return fmaxf(m, fabsf(
 // ---- any entries at all -------------------------------------------------------------
 // One block (rows x 128 columns of x, or of its transpose) by one workgroup,
 // entry by entry from memory and with the divider: blocks with infinities,
-// with scales below 2^-96, and matrices of fewer than eight columns.  Short
+// with very small scales, and matrices of fewer than eight columns.  Short
 // code, seldom run.
 template <int XT, bool E8M0, bool E5M2>
 __device__ __forceinline__ void quantize_slowly(const QuantArgs &g, int64_t r0, int64_t c0, bool square, bool transposed) {
@@ -223,7 +226,7 @@ __global__ __launch_bounds__(256) void quantize_rows_kernel(QuantArgs g) {
     }
     const Scale b = block_scale<E8M0, E5M2>(m);
     v2u w;
-    if (!E8M0 && (infinite || b.s < kSmallScale)) {
+    if (!E8M0 && (infinite || b.s < Format<E5M2>::small_scale)) {
         float y[8];
 #pragma unroll
         for (int i = 0; i < 8; i++) y[i] = v[i] / b.s;
@@ -276,7 +279,7 @@ __global__ __launch_bounds__(256) void quantize_tile_kernel(QuantArgs g) {
         __syncthreads();
         m = row_max(rmax[l16]);
         mine = block_scale<E8M0, E5M2>(m);
-        if (!(m <= kLargestFloat) || (!E8M0 && mine.s < kSmallScale)) {     // the same in every thread
+        if (!(m <= kLargestFloat) || (!E8M0 && mine.s < Format<E5M2>::small_scale)) {     // the same in every thread
             quantize_slowly<XT, E8M0, E5M2>(g, rb * 128, (int64_t)blk * 128, true, false);
             if (BOTH) quantize_slowly<XT, E8M0, E5M2>(g, (int64_t)blk * 128, rb * 128, true, true);
             return;
@@ -315,7 +318,7 @@ __global__ __launch_bounds__(256) void quantize_tile_kernel(QuantArgs g) {
         mine = block_scale<E8M0, E5M2>(m);
         div[tid] = mine.s;
         mul[tid] = mine.r;
-        const bool bad = !(m <= kLargestFloat) || (!E8M0 && mine.s < kSmallScale);
+        const bool bad = !(m <= kLargestFloat) || (!E8M0 && mine.s < Format<E5M2>::small_scale);
         if (__syncthreads_or(bad)) {
             quantize_slowly<XT, E8M0, E5M2>(g, rb * 128, (int64_t)blk * 128, false, false);
             quantize_slowly<XT, E8M0, E5M2>(g, (int64_t)blk * 128, rb * 128, false, true);
