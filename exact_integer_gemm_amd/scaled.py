@@ -10,7 +10,7 @@ powers of two as ``torch.float8_e8m0fnu``), one for each 128 columns of a row
     q, s = rg.block_quantize(x)                       # activations: one scale per row and 128 columns
     w, ws = rg.block_quantize(weight, block_rows=128)
     y = rg.scaled_mm_nt(q, s, w, ws)                  # x @ weight.T
-    lo, hi = rg.mm_enclose_nt(rg.dequantize(q, s), rg.dequantize(w, ws))   # what the product is, exactly enclosed
+    lo, hi = rg.mm_enclose_nt(rg.dequantize(q, s), rg.dequantize(w, ws))   # binary64 bounds of the exact product
     y = rg.scaled_linear(x, weight)                   # differentiable: both gradients are 8-bit products too
     y = rg.moe_layer(x, router, w_in, w_in_scales, w_out, w_out_scales, top_k=8)
 
@@ -138,15 +138,17 @@ def block_quantize_both(x: torch.Tensor, dtype: torch.dtype = torch.float8_e4m3f
 
 
 def dequantize(values: torch.Tensor, scales: torch.Tensor) -> torch.Tensor:
-    """The binary32 numbers that (values, scales) stand for (plain torch, for checks and for the enclosure)."""
+    """The numbers that (values, scales) stand for, exactly, in binary64 (plain torch, for checks and for the enclosure):
+    a value of four significant bits times a scale of 24 does not fit binary32."""
     rows, cols = values.shape
     f = scales
     if f.dtype != torch.float32:
-        e = f.contiguous().view(torch.uint8).int()
-        f = torch.where(e == 255, 0x7fc00000, torch.where(e > 0, e << 23, 1 << 22)).view(torch.float32)
+        e = f.contiguous().view(torch.uint8).long()
+        f = torch.where(e == 255, 0x7ff8 << 48, (e + (1023 - 127)) << 52).view(torch.float64)
+    f = f.double()
     if f.shape[0] != rows:
         f = f.repeat_interleave(SCALE_BLOCK, 0)[:rows]
-    return values.float() * f.repeat_interleave(SCALE_BLOCK, 1)[:, :cols]
+    return values.double() * f.repeat_interleave(SCALE_BLOCK, 1)[:, :cols]
 
 
 def _operand(values: torch.Tensor, scales: torch.Tensor, dtypes, name: str) -> Tuple[_Scaled, int, int]:

@@ -5,8 +5,9 @@
  *
  * The exact products of rns_gemm.h answer what a product is; these answer it
  * at the matrix cores' 8-bit rate, and rns_enclose.h tells how far such an
- * answer can be off: a block-scaled operand's entries are binary32 numbers
- * (value times scale), which the enclosure takes as they are.
+ * answer can be off: a block-scaled operand's entries (value times scale, up
+ * to 28 significant bits) are binary64 numbers, which the enclosure takes as
+ * they are.
  *
  * Conventions of rns_gemm.h: device pointers owned by the caller, launches
  * asynchronous on the caller's stream, no allocation, 0 or a negative RNS_E_*
