@@ -24,6 +24,7 @@ from dataclasses import dataclass
 from typing import Optional, Tuple
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import _Moe, _Scaled, _check, load
 
@@ -255,6 +256,7 @@ class _ScaledLinear(torch.autograd.Function):
         return y
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy):
         dy = dy.contiguous()
         g, gs, gt, gts = block_quantize_both(dy, dtype=ctx.grad_dtype, scale_dtype=ctx.saved.xt_scales.dtype)
@@ -267,7 +269,11 @@ class _ScaledLinear(torch.autograd.Function):
 def scaled_linear(x: torch.Tensor, weight: torch.Tensor, scale_dtype: torch.dtype = torch.float8_e8m0fnu,
                   grad_dtype: torch.dtype = torch.float8_e4m3fn) -> torch.Tensor:
     """``scaled_linear_forward`` as a differentiable function; the gradients are those of
-    ``scaled_linear_backward`` (the quantisation is passed through), in the operands' dtypes."""
+    ``scaled_linear_backward`` (the quantisation is passed through), in the operands' dtypes.
+
+    First derivatives by ``backward`` only: differentiating the gradients again raises, and there is no rule for
+    forward mode or ``vmap``.
+    """
     return _ScaledLinear.apply(x, weight, scale_dtype, grad_dtype)
 
 

@@ -1,0 +1,73 @@
+"""The differentiable linear layer as autograd sees it.  On the CPU the quantiser
+and the product stand in as plain torch (what is tested is which of them are
+called, and what is kept); on the GPU they are the kernels."""
+import numpy as np
+import pytest
+import torch
+
+import exact_integer_gemm_amd as rg
+from exact_integer_gemm_amd import scaled
+
+M, N, K = 5, 7, 6
+
+
+class Stand:
+    """Stand-ins that keep entries as they are, with scales of one, and count calls."""
+
+    def __init__(self):
+        self.calls = []
+
+    def block_quantize(self, x, dtype=None, block_rows=1, scale_dtype=torch.float32):
+        self.calls.append("one")
+        return x.detach().clone(), torch.ones(1, 1, dtype=scale_dtype)
+
+    def block_quantize_both(self, x, dtype=None, block_rows=1, scale_dtype=torch.float32):
+        self.calls.append("both")
+        one = torch.ones(1, 1, dtype=scale_dtype)
+        return x.detach().clone(), one, x.detach().t().contiguous(), one.clone()
+
+    def scaled_mm_nt(self, a, a_scales, b, b_scales, out_dtype=torch.bfloat16, out=None, workspace=None):
+        self.calls.append("mm")
+        return (a @ b.t()).to(out_dtype)
+
+
+@pytest.fixture(params=["stand", pytest.param("gpu", marks=pytest.mark.gpu)])
+def layer(request, monkeypatch):
+    """(device, the stand-ins or None)."""
+    if request.param == "gpu":
+        return "cuda", None
+    stand = Stand()
+    for name in ("block_quantize", "block_quantize_both", "scaled_mm_nt"):
+        monkeypatch.setattr(scaled, name, getattr(stand, name))
+    return "cpu", stand
+
+
+def operands(device, x_grad=True, w_grad=True):
+    g = torch.Generator().manual_seed(1)
+    x, w = torch.randn((M, K), generator=g).to(device), torch.randn((N, K), generator=g).to(device)
+    return x.requires_grad_(x_grad), w.requires_grad_(w_grad)
+
+
+def run(x, w):
+    return rg.scaled_linear(x, w, scale_dtype=torch.float32)
+
+
+def test_gradients_reach_both_operands(layer):
+    device, stand = layer
+    x, w = operands(device)
+    dy = torch.randn((M, N), generator=torch.Generator().manual_seed(2)).to(device)
+    run(x, w).backward(dy)
+    # the kernels' operands are off by at most half a step of e4m3, 2^-4, each
+    tol = 1e-6 if stand else 2 * 2.0 ** -4 + 2.0 ** -8
+    for got, want, size in ((x.grad, dy @ w, dy.abs() @ w.abs()), (w.grad, dy.t() @ x, dy.abs().t() @ x.abs())):
+        assert bool(((got - want).abs() <= tol * size + 1e-6).all())
+
+
+def test_second_derivatives_are_refused(layer):
+    """A gradient penalty would lose its term without a word."""
+    device, _ = layer
+    x, w = operands(device)
+    gx, = torch.autograd.grad(run(x, w).square().sum(), x, create_graph=True)
+    penalty = gx.square().sum() + (w * w).sum()
+    with pytest.raises(RuntimeError, match="twice|once_differentiable"):
+        penalty.backward()
