@@ -248,21 +248,28 @@ def scaled_linear_backward(saved: LinearSaved, dy: torch.Tensor, grad_dtype: tor
             scaled_mm_nt(gt, gts, saved.xt, saved.xt_scales, out_dtype=dw_dtype))
 
 
+def _whole(t: torch.Tensor) -> torch.Tensor:
+    """An operand with the padding behind its rows, as the quantiser made it: so it keeps its layout where a saved tensor
+    is copied."""
+    return t if t._base is None else t._base
+
+
 class _ScaledLinear(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weight, scale_dtype, grad_dtype):
-        y, saved = scaled_linear_forward(x, weight, scale_dtype)
-        ctx.saved, ctx.grad_dtype, ctx.dw_dtype = saved, grad_dtype, weight.dtype
+        y, k = scaled_linear_forward(x, weight, scale_dtype)
+        ctx.save_for_backward(_whole(k.xt), k.xt_scales, _whole(k.wt), k.wt_scales)
+        ctx.x_dtype, ctx.dw_dtype, ctx.scale_dtype, ctx.grad_dtype = x.dtype, weight.dtype, scale_dtype, grad_dtype
         return y
 
     @staticmethod
     @once_differentiable
     def backward(ctx, dy):
-        dy = dy.contiguous()
-        g, gs, gt, gts = block_quantize_both(dy, dtype=ctx.grad_dtype, scale_dtype=ctx.saved.xt_scales.dtype)
-        k = ctx.saved
-        dx = scaled_mm_nt(g, gs, k.wt, k.wt_scales, out_dtype=k.x_dtype) if ctx.needs_input_grad[0] else None
-        dw = scaled_mm_nt(gt, gts, k.xt, k.xt_scales, out_dtype=ctx.dw_dtype) if ctx.needs_input_grad[1] else None
+        xt, xts, wt, wts = ctx.saved_tensors
+        xt, wt = xt[:, :dy.shape[0]], wt[:, :dy.shape[1]]
+        g, gs, gt, gts = block_quantize_both(dy.contiguous(), dtype=ctx.grad_dtype, scale_dtype=ctx.scale_dtype)
+        dx = scaled_mm_nt(g, gs, wt, wts, out_dtype=ctx.x_dtype) if ctx.needs_input_grad[0] else None
+        dw = scaled_mm_nt(gt, gts, xt, xts, out_dtype=ctx.dw_dtype) if ctx.needs_input_grad[1] else None
         return dx, dw, None, None
 
 

@@ -71,3 +71,50 @@ def test_second_derivatives_are_refused(layer):
     penalty = gx.square().sum() + (w * w).sum()
     with pytest.raises(RuntimeError, match="twice|once_differentiable"):
         penalty.backward()
+
+
+def test_what_is_kept_goes_through_the_graph(layer):
+    """Hooks on saved tensors (offloading, checkpointing) see it, and a backward pass frees it."""
+    device, _ = layer
+    x, w = operands(device)
+    seen = []
+    with torch.autograd.graph.saved_tensors_hooks(lambda t: seen.append(t.shape) or t, lambda t: t):
+        y = run(x, w)
+    assert sum(s[0] == K and s[1] >= M for s in seen) == 2       # x and the weight, transposed
+    y.sum().backward()
+    with pytest.raises(RuntimeError, match="second time"):
+        y.sum().backward()
+    x.grad = w.grad = None
+    y = run(x, w)
+    y.sum().backward(retain_graph=True)
+    first = x.grad.clone(), w.grad.clone()
+    y.sum().backward()
+    assert torch.equal(x.grad, 2 * first[0]) and torch.equal(w.grad, 2 * first[1])
+
+
+@pytest.mark.gpu
+def test_what_is_kept_may_leave_the_device():
+    """Kept on the host until it is needed, to the same bits."""
+    g = torch.Generator().manual_seed(3)
+    x, w, dy = (torch.randn(s, generator=g).cuda() for s in ((70, 200), (90, 200), (70, 90)))
+    x.requires_grad_(), w.requires_grad_()
+    run(x, w).backward(dy)
+    here = x.grad, w.grad
+    x.grad = w.grad = None
+    with torch.autograd.graph.save_on_cpu():
+        y = run(x, w)
+    y.backward(dy)
+    assert torch.equal(x.grad, here[0]) and torch.equal(w.grad, here[1])
+
+
+def test_recomputed_layers(layer):
+    """Non-reentrant checkpointing gives the gradients of the plain pass."""
+    from torch.utils.checkpoint import checkpoint
+    device, _ = layer
+    grads = []
+    for again in (False, True):
+        x, w = operands(device)
+        y = checkpoint(run, x, w, use_reentrant=False) if again else run(x, w)
+        y.square().sum().backward()
+        grads.append((x.grad, w.grad))
+    assert all(torch.equal(a, b) for a, b in zip(*grads))
