@@ -230,13 +230,24 @@ class LinearSaved:
     x_dtype: torch.dtype
 
 
+def _oriented(t: torch.Tensor, transposed: bool, **how):
+    """(values, scales, values_t, scales_t) of t, the last two None unless they are wanted."""
+    return block_quantize_both(t, **how) if transposed else (*block_quantize(t, **how), None, None)
+
+
+def _forward(x, weight, scale_dtype, x_transposed: bool, weight_transposed: bool):
+    """y, and x and the weight transposed where they are wanted."""
+    q, s, *xt = _oriented(x, x_transposed, scale_dtype=scale_dtype)
+    w, ws, *wt = _oriented(weight, weight_transposed, block_rows=SCALE_BLOCK, scale_dtype=scale_dtype)
+    return scaled_mm_nt(q, s, w, ws, out_dtype=x.dtype), *xt, *wt
+
+
 def scaled_linear_forward(x: torch.Tensor, weight: torch.Tensor,
                           scale_dtype: torch.dtype = torch.float8_e8m0fnu) -> Tuple[torch.Tensor, LinearSaved]:
     """y = x @ weight.T for x [M, K], weight [N, K], in 8-bit products: x with a scale for each row and 128 columns,
     the weight with one for each 128 x 128 block.  Returns y in x's dtype and what the gradients need."""
-    q, s, qt, st = block_quantize_both(x, scale_dtype=scale_dtype)
-    w, ws, wt, wts = block_quantize_both(weight, block_rows=SCALE_BLOCK, scale_dtype=scale_dtype)
-    return scaled_mm_nt(q, s, w, ws, out_dtype=x.dtype), LinearSaved(qt, st, wt, wts, x.dtype)
+    y, *saved = _forward(x, weight, scale_dtype, True, True)
+    return y, LinearSaved(*saved, x.dtype)
 
 
 def scaled_linear_backward(saved: LinearSaved, dy: torch.Tensor, grad_dtype: torch.dtype = torch.float8_e4m3fn,
@@ -248,17 +259,19 @@ def scaled_linear_backward(saved: LinearSaved, dy: torch.Tensor, grad_dtype: tor
             scaled_mm_nt(gt, gts, saved.xt, saved.xt_scales, out_dtype=dw_dtype))
 
 
-def _whole(t: torch.Tensor) -> torch.Tensor:
+def _whole(t: Optional[torch.Tensor]) -> Optional[torch.Tensor]:
     """An operand with the padding behind its rows, as the quantiser made it: so it keeps its layout where a saved tensor
     is copied."""
-    return t if t._base is None else t._base
+    return t if t is None or t._base is None else t._base
 
 
 class _ScaledLinear(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, x, weight, scale_dtype, grad_dtype):
-        y, k = scaled_linear_forward(x, weight, scale_dtype)
-        ctx.save_for_backward(_whole(k.xt), k.xt_scales, _whole(k.wt), k.wt_scales)
+    def forward(ctx, x, weight, scale_dtype, grad_dtype, tracked):
+        # x's transpose serves the weight's gradient, the weight's serves x's
+        need_dx, need_dw = (tracked and need for need in ctx.needs_input_grad[:2])
+        y, xt, xts, wt, wts = _forward(x, weight, scale_dtype, need_dw, need_dx)
+        ctx.save_for_backward(_whole(xt), xts, _whole(wt), wts)
         ctx.x_dtype, ctx.dw_dtype, ctx.scale_dtype, ctx.grad_dtype = x.dtype, weight.dtype, scale_dtype, grad_dtype
         return y
 
@@ -266,11 +279,11 @@ class _ScaledLinear(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, dy):
         xt, xts, wt, wts = ctx.saved_tensors
-        xt, wt = xt[:, :dy.shape[0]], wt[:, :dy.shape[1]]
-        g, gs, gt, gts = block_quantize_both(dy.contiguous(), dtype=ctx.grad_dtype, scale_dtype=ctx.scale_dtype)
-        dx = scaled_mm_nt(g, gs, wt, wts, out_dtype=ctx.x_dtype) if ctx.needs_input_grad[0] else None
-        dw = scaled_mm_nt(gt, gts, xt, xts, out_dtype=ctx.dw_dtype) if ctx.needs_input_grad[1] else None
-        return dx, dw, None, None
+        need_dx, need_dw = ctx.needs_input_grad[:2]
+        g, gs, gt, gts = _oriented(dy.contiguous(), need_dw, dtype=ctx.grad_dtype, scale_dtype=ctx.scale_dtype)
+        dx = scaled_mm_nt(g, gs, wt[:, :dy.shape[1]], wts, out_dtype=ctx.x_dtype) if need_dx else None
+        dw = scaled_mm_nt(gt, gts, xt[:, :dy.shape[0]], xts, out_dtype=ctx.dw_dtype) if need_dw else None
+        return dx, dw, None, None, None
 
 
 def scaled_linear(x: torch.Tensor, weight: torch.Tensor, scale_dtype: torch.dtype = torch.float8_e8m0fnu,
@@ -278,10 +291,11 @@ def scaled_linear(x: torch.Tensor, weight: torch.Tensor, scale_dtype: torch.dtyp
     """``scaled_linear_forward`` as a differentiable function; the gradients are those of
     ``scaled_linear_backward`` (the quantisation is passed through), in the operands' dtypes.
 
-    First derivatives by ``backward`` only: differentiating the gradients again raises, and there is no rule for
-    forward mode or ``vmap``.
+    Operands are quantised in the orientations that the wanted gradients need.  First derivatives by ``backward`` only:
+    differentiating the gradients again raises, and there is no rule for forward mode or ``vmap``.
     """
-    return _ScaledLinear.apply(x, weight, scale_dtype, grad_dtype)
+    # within the function gradients are off, whatever the caller's mode is
+    return _ScaledLinear.apply(x, weight, scale_dtype, grad_dtype, torch.is_grad_enabled())
 
 
 # ---- mixture of experts ----------------------------------------------------------------

@@ -1,7 +1,6 @@
 """The differentiable linear layer as autograd sees it.  On the CPU the quantiser
 and the product stand in as plain torch (what is tested is which of them are
 called, and what is kept); on the GPU they are the kernels."""
-import numpy as np
 import pytest
 import torch
 
@@ -118,3 +117,42 @@ def test_recomputed_layers(layer):
         y.square().sum().backward()
         grads.append((x.grad, w.grad))
     assert all(torch.equal(a, b) for a, b in zip(*grads))
+
+
+@pytest.mark.parametrize("x_grad,w_grad,grad_mode,forward,backward", [
+    (True, True, True, ["both", "both", "mm"], ["both", "mm", "mm"]),
+    (True, False, True, ["one", "both", "mm"], ["one", "mm"]),         # a frozen weight: dy along N, the weight transposed
+    (False, True, True, ["both", "one", "mm"], ["both", "mm"]),        # the first layer
+    (False, False, True, ["one", "one", "mm"], None),
+    (True, True, False, ["one", "one", "mm"], None),                   # inference
+])
+def test_only_what_the_gradients_need_is_quantised(layer, x_grad, w_grad, grad_mode, forward, backward):
+    device, stand = layer
+    x, w = operands(device)
+    want = run(x, w)
+    want.square().sum().backward()
+    gx, gw = x.grad, w.grad
+    x, w = operands(device, x_grad, w_grad)
+    if stand:
+        stand.calls.clear()
+    with torch.set_grad_enabled(grad_mode):
+        y = run(x, w)
+    assert torch.equal(y, want) and y.requires_grad == (backward is not None)
+    if stand:
+        assert stand.calls == forward
+        stand.calls.clear()
+    if backward is None:
+        return
+    y.square().sum().backward()
+    assert (x.grad is None) == (not x_grad) and (w.grad is None) == (not w_grad)
+    assert (x.grad is None or torch.equal(x.grad, gx)) and (w.grad is None or torch.equal(w.grad, gw))
+    assert stand is None or stand.calls == backward
+
+
+def test_other_modes_are_refused(layer):
+    device, _ = layer
+    x, w = operands(device, False, False)
+    with torch.autograd.forward_ad.dual_level(), pytest.raises((RuntimeError, NotImplementedError)):
+        run(torch.autograd.forward_ad.make_dual(x, torch.ones_like(x)), w)
+    with pytest.raises((RuntimeError, NotImplementedError)):
+        torch.vmap(lambda t: run(t, w))(x.unsqueeze(0))
