@@ -86,6 +86,17 @@ def _rows_of(t: torch.Tensor, name: str) -> Tuple[int, int, int]:
     return rows, cols, ld
 
 
+def _scratch(workspace: torch.Tensor, device: torch.device) -> Tuple[int, int]:
+    """(address, bytes) of a caller's workspace."""
+    if not isinstance(workspace, torch.Tensor):
+        raise TypeError("workspace must be a torch.Tensor")
+    if workspace.device != device:
+        raise ValueError(f"workspace must be on {device}, got {workspace.device}")
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
 def _quantize(x, dtype, block_rows, scale_dtype, both):
     _gpu(x, _WIDE, "x")
     if dtype not in _VALUES:
@@ -211,10 +222,7 @@ def scaled_mm_nt(a: torch.Tensor, a_scales: torch.Tensor, b: torch.Tensor, b_sca
         _check(load().rns_scaled_workspace_size(M, N, K, A, B, need), "rns_scaled_workspace_size")
         if need.value:
             workspace = torch.empty(need.value, dtype=torch.uint8, device=a.device)
-    if workspace is None:
-        ws, ws_bytes = None, 0
-    else:
-        ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    ws, ws_bytes = (None, 0) if workspace is None else _scratch(workspace, a.device)
     _launch("rns_scaled_mm_nt", a.device, M, N, K, A, B, out.data_ptr(), _TYPES[out.dtype], ldy, ws, ws_bytes)
     return out
 
@@ -359,7 +367,7 @@ def moe_layer(x: torch.Tensor, router: torch.Tensor, w_in: torch.Tensor, w_in_sc
                 w_out_scales.data_ptr(), w_in_scales.stride(), w_out_scales.stride(),
                 out.data_ptr(), ids.data_ptr() if return_routing else None,
                 probs.data_ptr() if return_routing else None)
-    _launch("rns_moe_layer", dev, args, workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    _launch("rns_moe_layer", dev, args, *_scratch(workspace, dev))
     return (out, ids, probs) if return_routing else out
 
 
