@@ -627,6 +627,8 @@ int rns_moe_layer(const rns_moe_t *args, void *ws, size_t ws_bytes, hipStream_t 
         if (a.si[i] < 0 || (i < 3 && a.so[i] < 0)) return RNS_E_ARG;
     if (a.T == 0) return RNS_OK;
     if (!a.x || !a.router || !a.w_in || !a.w_in_scales || !a.w_out || !a.w_out_scales || !a.y || !ws) return RNS_E_ARG;
+    if (a.scale_type == RNS_T_F32 && ((uintptr_t)a.w_in_scales | (uintptr_t)a.w_out_scales) % 4) return RNS_E_ARG;
+    if (((uintptr_t)a.ids | (uintptr_t)a.probs) % 4) return RNS_E_ARG;
     if (((uintptr_t)a.x | (uintptr_t)a.router | (uintptr_t)a.w_in | (uintptr_t)a.w_out | (uintptr_t)a.y) % 16 ||
         (uintptr_t)ws % 256)
         return RNS_E_ARG;

@@ -1013,6 +1013,7 @@ bool operand_ok(const rns_scaled_t *o, int64_t rows, int64_t K) {
     if (!o || (o->type != RNS_T_E4M3 && o->type != RNS_T_E5M2)) return false;
     if (o->scale_type != RNS_T_F32 && o->scale_type != RNS_T_E8M0) return false;
     if (o->block_rows != 1 && o->block_rows != 128) return false;
+    if (o->scale_type == RNS_T_F32 && (uintptr_t)o->scales % 4) return false;
     return o->ld >= K && o->ld <= RNS_SCALED_LD_MAX && o->s_row >= 0 && o->s_blk >= 0 && rows >= 0;
 }
 

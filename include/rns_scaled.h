@@ -11,7 +11,8 @@
  *
  * Conventions of rns_gemm.h: device pointers owned by the caller, launches
  * asynchronous on the caller's stream, no allocation, 0 or a negative RNS_E_*
- * code, nothing written on a validation error.
+ * code, nothing written on a validation error.  Arrays of binary32 and int32
+ * lie on 4-byte boundaries.
  *
  * The format
  * ----------
