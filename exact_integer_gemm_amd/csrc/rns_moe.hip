@@ -424,8 +424,8 @@ __global__ __launch_bounds__(kInThreads) void moe_in_kernel(MoeArgs g) {
 // experts.  A wave fetches a few blocks ahead and adds each one's products to
 // its own copy of the 16 entries in LDS; the copies are added in wave order.
 // A token outside an expert has no part in its products.  1 token (as above):
-// 11.3 us for 17 MB, a launch, the table and the first bytes' way 7 of them; 32
-// tokens: 74 us for 238 MB, 3.2 TB/s.
+// 11.7 us for 17 MB, a launch, the table and the first bytes' way 7 of them; 32
+// tokens: 75 us for 238 MB, 3.2 TB/s.
 constexpr int kOutWaves = 8, kOutThreads = kOutWaves * 64;
 constexpr int kWeights = 4, kColumns = 2;                   // blocks fetched ahead: weights from memory, activations from L2
 
@@ -645,7 +645,7 @@ int rns_moe_layer(const rns_moe_t *args, void *ws, size_t ws_bytes, hipStream_t 
     // as many workgroups as stay resident, each with several items where there are more
     const int64_t items = (int64_t)(a.T * a.top_k < a.E ? a.T * a.top_k : a.E) * div_up(a.I, 16);
     // At most two workgroups to a compute unit, which go on to further items: each works out the routing for itself.  32
-    // tokens of 64 experts, H 4096, I 1040: 179 us; at most 256 workgroups 202, 1024 187, 4096 262.
+    // tokens of 64 experts, H 4096, I 1040, the layer's GPU time: 182 us; at most 256 workgroups 206, 1024 191, 4096 266.
     const dim3 in_grid((unsigned)(items < 512 ? items : 512)), out_grid((unsigned)(a.H / 16));
     if (a.scale_type == RNS_T_F32) {
         hipLaunchKernelGGL((moe_in_kernel<RNS_T_F32>), in_grid, dim3(kInThreads), 0, stream, g);

@@ -161,10 +161,13 @@ __device__ __forceinline__ v4u clear_tail(v4u w, int k, int K) {
 // operand: a lane's four sums belong to one token and four neighbouring columns
 // of Y.  The waves' sums meet in LDS and are added in wave order.
 //
-// 1 x 4096 x 4096, bfloat16 outputs: 5.7 us (f32 scales; e8m0 6.5), of which a
-// launch is 2.3 and the weight at a copy's rate 3.6; 1 x 16384 x 8192: 24 us,
-// 5.6 TB/s.  32 rows of b to a workgroup halve what is read of a, which comes
-// from L2, and were slower (4096 x 4096: 7.3 us).
+// Exponent scales are the instruction's own, one load for a's and one for b's;
+// binary32 scales are applied by significands and exponents, beside the memory.
+// 1 x 4096 x 4096, bfloat16 outputs, on a weight that has left the caches: 6.8
+// us of GPU time (e8m0 5.9), of which a launch is 2.3 and the weight at a
+// copy's rate 3.6; 1 x 16384 x 8192: 27 us, 5.0 TB/s.  32 rows of b to a
+// workgroup halve what is read of a, which comes from L2, and were slower (7.3
+// us where 16 took 5.4).
 constexpr int kSkinnyBlocks = 2, kSkinnyAhead = 2;
 struct Frag {
     v4u lo, hi;
@@ -313,8 +316,10 @@ __global__ __launch_bounds__(1024) void mm_skinny_kernel(MmArgs g) {
 //
 // A block's fragments cost more to read from LDS (T = 128: 96 KiB at 128 bytes
 // a clock, 0.32 us) than to multiply (0.21 us at the instructions' rate);
-// measured, a block takes 0.57 us (both arrays powers of two) to 0.9.  2048 x
-// 2048 x 4096, one tile to a compute unit: 24 us; binary32 scales 29.
+// measured, a block takes 0.65 us (both arrays powers of two) to 0.85, and 1.5
+// to 1.8 with a binary32 result.  2048 x 2048 x 4096, one tile to a compute unit:
+// 24 us; binary32 scales 27, those of single rows of b 30; binary32 results 51
+// and 58.
 __device__ __attribute__((aligned(16))) const uint32_t kZeros[4] = {0, 0, 0, 0};
 
 __device__ __forceinline__ int swz8(int row) { return (row ^ (row >> 3)) & 7; }
@@ -690,10 +695,11 @@ __global__ __launch_bounds__(T * 4 * KG) void mm_tile_kernel(MmArgs g) {
 // phase's last three are left to the following read phase, which has time to
 // spare.
 //
-// The matrix cores bound it: 8192 x 8192 x 8192 in 450 to 500 us (both arrays
-// powers of two, 2.2 to 2.4 PFLOP/s), 520 with binary32 scales, whose vector
-// instructions share the issue slots; the library's product with one scale for
-// each whole operand takes 390 to 430.  4096 x 4096 x 4096: 61 us, 51 there.
+// The matrix cores bound it: 8192 x 8192 x 8192 in 400 to 500 us (both arrays
+// powers of two, 2.2 to 2.7 PFLOP/s), 540 to 620 with binary32 scales, whose
+// vector instructions share the issue slots (taking each scale apart is 3% of
+// it); the library's product with one scale for each whole operand takes 390 to
+// 430.  4096 x 4096 x 4096: 57 to 61 us, 83 with binary32 scales, 51 there.
 // b times a, times 2^(eb - 127) and 2^(byte i of ea - 127).
 template <int AT>
 __device__ __forceinline__ v4f scaled_product(const v8i &b, const v8i &a, int i, uint32_t eb, uint32_t ea) {
@@ -1045,17 +1051,19 @@ bool aligned(const rns_scaled_t *o) {
 MmPlan plan_mm(int64_t M, int64_t N, int64_t K, const rns_scaled_t *a, const rns_scaled_t *b, bool wide) {
     MmPlan p{kGeneral, 1, 0, 0};
     if (M == 0 || N == 0 || K == 0 || !aligned(a) || !aligned(b)) return p;
-    // Up to 16 rows read the weight straight into registers: 16 x 4096 x 4096 in 7.6 us, against 9.1 in tiles of 64
-    // that split the contraction (17 rows are two passes of it: 12 against 9.5).  With over 8 rows and much of a weight
-    // to read the tiles win, whose rows of a are not fetched again for every 16 of b: 16 x 16384 x 8192 in 25 us
-    // against 34, 16 x 1024 x 16384 in 12.5 against 18.  At twice the instructions, for 32-bit outputs, they do not.
+    // Figures here: GPU time of one product among others, on operands that have left the caches where those are small.
+    // Up to 16 rows read the weight straight into registers: 16 x 4096 x 4096 in 7.5 us, against 10.4 in tiles of 64
+    // that split the contraction.  With over 8 rows and much of a weight to read the tiles win, whose rows of a are not
+    // fetched again for every 16 of b: 16 x 16384 x 8192 in 34 us against 36, 16 x 1024 x 16384 in 12.8 against 18.
+    // At twice the instructions, for 32-bit outputs, they do not (16 x 4096 x 4096 in 14 against 7.7).
     if (M <= 16 && (wide || M <= 8 || (N * K < (int64_t)1 << 26 && K <= 8192))) {
         p.path = kSkinny;
         return p;
     }
     // Tiles of 256 where those of 128 take more than twice as many rounds of the chip: 3328 x 3328 x 4096 (one round
-    // against three) in 48 us against 63, with binary32 scales 67 against 80; 2816 x 2816 x 4096 (one against two) in 46
-    // against 45, and 66 against 55.  They have no form for 32-bit outputs, nor for binary32 scales of single rows of b,
+    // against three) in 52 us against 66, with binary32 scales 74 against 75; 2816 x 2816 x 4096 (one against two) in 50
+    // against 45, and 72 against 52.  Of two blocks only, 8192 x 8192 x 256 takes 48 against 72, but with binary32 scales
+    // 87 against 75.  They have no form for 32-bit outputs, nor for binary32 scales of single rows of b,
     // and scale offsets inside a tile are 32-bit there.
     const int cus = device_cus();
     const int64_t far = (int64_t)1 << 20;
@@ -1064,15 +1072,16 @@ MmPlan plan_mm(int64_t M, int64_t N, int64_t K, const rns_scaled_t *a, const rns
         p.path = kBig;
         return p;
     }
-    // Tiles of 64 where those of 128 would fill at most half of the chip: 777 x 1100 x 650 in 7.3 us against 11.0, 512 x
-    // 4096 x 4096 in 18 against 23; but 1000 x 3001 x 1537, three quarters of the chip, in 16.9 against 15.1.  And where
-    // the rows do not fill half of one: 48 x 32768 x 4096 in 35 us against 40.
+    // Tiles of 64 where those of 128 would fill at most half of the chip: 777 x 1100 x 650 in 7.1 us against 11.2, 512 x
+    // 4096 x 4096 in 18 against 21 (binary32 scales 20 against 25); but 1000 x 3001 x 1537, three quarters of the chip,
+    // in 19.6 against 16.7.  And where the rows do not fill half of one: 48 x 32768 x 4096 in 34 us against 39.
     const int64_t blocks = div_up(K, 128);
     p.path = M <= 64 || div_up(M, 128) * div_up(N, 128) * 2 <= cus ? kSmall : kTile;
     // Where those are at most one to a compute unit, a tile's workgroup is two groups of waves that share its blocks (1024
-    // x 1024 x 8192 in 21 us against 24 in two launches; 777 x 1100 x 650 in 7.8 against 8.3, binary32 scales), and
+    // x 1024 x 8192 in 19 us against 24 by one group; 777 x 1100 x 650 in 7.1 against 7.5, binary32 scales), and
     // where they are at most one to two units the contraction is split besides, while each part keeps at least 16
-    // blocks: 48 x 8192 x 4096 in 14.3 us against 15.8; parts of eight: 48 x 2048 x 2048 in 8.8 us against 7.8.
+    // blocks: 48 x 8192 x 4096 in 14.0 us against 14.6, 64 x 4096 x 8192 in 14.8 against 23.6; parts of eight: 48 x 2048
+    // x 2048 in 9.0 us against 8.3.
     const int64_t tiles = div_up(M, 64) * div_up(N, 64);
     if (p.path == kSmall && tiles <= cus && blocks >= 2) {
         p.path = kPair;

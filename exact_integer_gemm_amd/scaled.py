@@ -196,7 +196,8 @@ def scaled_mm_nt(a: torch.Tensor, a_scales: torch.Tensor, b: torch.Tensor, b_sca
 
     b is float8_e4m3fn, a either type; both scale arrays are of one type and
     may have any strides.  Sums are binary32, rounded once to ``out_dtype``
-    (bfloat16, float16 or float32).  Rows on 16-byte boundaries, as the
+    (bfloat16, float16 or float32); for the 16-bit types each product is kept to
+    about 2^-14 of the largest of the 64 or 128 added at a time.  Rows on 16-byte boundaries, as the
     quantiser lays them out, are read fastest; others are read as they lie.
     """
     A, M, K = _operand(a, a_scales, _VALUES, "a")

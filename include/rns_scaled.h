@@ -98,7 +98,8 @@ int rns_block_quantize(int64_t R, int64_t C, const void *x, int32_t x_type, int6
  * 2^-120 is kept to 2^-144.  For y_type RNS_T_F32 the inner sums are binary32
  * sums of exact products; for the 16-bit types they are the 8-bit matrix
  * instructions', which keep each product to about 2^-14 of the largest of the
- * 64 or 128 added at a time.  b's values are
+ * 64 or 128 added at a time (sums whose terms cancel to less than that want y
+ * in binary32).  b's values are
  * RNS_T_E4M3, a's either type; both scale arrays are of one type.
  *
  * Operands are read in place.  Rows on 16-byte boundaries, readable to the next
